@@ -24,6 +24,7 @@
 #include <climits>
 
 #include "kernels.cuh"
+#include "q8_ahead.cuh"
 
 namespace lfm3 {
 
@@ -306,9 +307,13 @@ __global__ void __launch_bounds__(Q8_THREADS, Q8Shape<NT>::RESIDENT)
     f.page = f.pages - 1 - i % f.pages;
     return f;
   };
-  // Tile k of this warp: quarter `warp` of page-head lo + k. Lanes look 32 tiles up at a time, up to a batch ahead:
-  // the row of the tile in the pool (-1: not a tile of codes) and its scales.
-  struct Batch { int row; float ks, vs; };
+  // Tile k of this warp: quarter `warp` of page-head lo + k. Lanes look 32 tiles up at a time, up to a batch ahead (Q8Ahead):
+  // the row of the tile in the pool (-1: not a tile of codes, or behind the share) and its scales.
+  struct Batch {
+    int at;
+    float ks, vs;
+    DEVI int row(int i) const { return __shfl_sync(0xffffffffu, at, i); }
+  };
   auto look_up = [&](int k0) -> Batch {
     Batch x{-1, 0.f, 0.f};
     const int r = lo + k0 + lane;
@@ -317,7 +322,7 @@ __global__ void __launch_bounds__(Q8_THREADS, Q8Shape<NT>::RESIDENT)
       if (4 * f.page + warp < lens[f.stream] / QBLK) {
         const int page = __ldcg(A.table + (size_t)slots[f.stream] * A.max_pages + f.page);
         const int tile = page * HKV + f.hg / A.groups;
-        x.row = tile * PAGE + warp * QBLK;
+        x.at = tile * PAGE + warp * QBLK;
         x.ks = __ldcg(A.k_scale + (size_t)tile * (PAGE / QBLK) + warp);
         x.vs = __ldcg(A.v_scale + (size_t)tile * (PAGE / QBLK) + warp);
       }
@@ -339,9 +344,9 @@ __global__ void __launch_bounds__(Q8_THREADS, Q8Shape<NT>::RESIDENT)
     }
   };
   if (lo < hi) request_q(find(lo));
-  Batch cur = look_up(0), nxt{-1, 0.f, 0.f};
-  auto fetch = [&](int k, int from, int place) {  // tile k (in the batch of tile `from` or the next one) into that ring place
-    const int row = __shfl_sync(0xffffffffu, (k ^ from) & ~31 ? nxt.row : cur.row, k & 31);
+  Q8Ahead<Batch> ahead{look_up(0), Batch{-1, 0.f, 0.f}};
+  auto fetch = [&](int k, int present, int place) {  // tile k into that ring place
+    const int row = ahead.row(k, present);
     if (row >= 0 && lane == 0) {
       const uint32_t bar = su32(&bars[warp][place]), dst = base + place * 2 * Q8_TILE;
       mbar_expect_tx(bar, 2 * Q8_TILE);
@@ -504,8 +509,7 @@ __global__ void __launch_bounds__(Q8_THREADS, Q8Shape<NT>::RESIDENT)
 
     // ---- this warp's tiles of the segment
     auto next_tile = [&]() {
-      if ((k & 31) == 0 && lo + k + 32 < hi) nxt = look_up(k + 32);
-      if ((k & 31) == 31) cur = nxt;
+      ahead.done(k, look_up);
       ++k;
       at = at + 1 == D ? 0 : at + 1;
     };
@@ -623,7 +627,7 @@ __global__ void __launch_bounds__(Q8_THREADS, Q8Shape<NT>::RESIDENT)
       ok = __all_sync(0xffffffffu, mbar_wait(su32(&bars[warp][at]), (par >> at) & 1, A.err));
       if (!ok) continue;
       par ^= 1u << at;
-      tile(base + at * 2 * Q8_TILE, __shfl_sync(0xffffffffu, cur.ks, k & 31), __shfl_sync(0xffffffffu, cur.vs, k & 31), 0, std::true_type{});
+      tile(base + at * 2 * Q8_TILE, __shfl_sync(0xffffffffu, ahead.cur.ks, k & 31), __shfl_sync(0xffffffffu, ahead.cur.vs, k & 31), 0, std::true_type{});
       fetch(k + D, k, at);
     }
 
