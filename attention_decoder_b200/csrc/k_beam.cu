@@ -95,6 +95,9 @@ __global__ void __launch_bounds__(BM_THREADS) k_beam_parts(const float* __restri
   if (mk > ORD_NEG_INF) {
 #pragma unroll
     for (int k = 0; k < 4 * IT; ++k) s += ex2_ftz((v[k] - m) * 1.4426950408889634f);
+  } else {  // nothing above -inf: a NaN, which no maximum shows, still has to reach the row's sum
+#pragma unroll
+    for (int k = 0; k < 4 * IT; ++k) s = v[k] != v[k] ? v[k] : s;
   }
   s = warp_sum(s);
   if (lane == 0) wsum[warp] = s;

@@ -145,6 +145,23 @@ def test_finished_beams_offer_one_token(select):
 
 
 @gpu
+def test_a_nan_among_masked_tokens_counts(select):
+    """A NaN with nothing but -inf around it, one after the last whole part of a row, and a stretch of nothing else."""
+    x, s = draw(3, 4, 5001, 21)
+    x[0, 1, 100:] = float("-inf")
+    x[0, 1, 3333] = float("nan")
+    x[1, 2, 900:5000] = float("nan")
+    x[2, :, 2000:] = float("-inf")
+    x[2, 3, 5000] = float("nan")
+    s[0, 1] = s[1, 2] = s[2, 3] = 0.0                           # (they would come first)
+    check(select, x, s, 10)
+    for offset in range(4):
+        x, s = draw(1, 3, 1025 + offset, 22, 0, offset)
+        x[0, 1, -1], s[0, 1] = float("nan"), 0.0
+        check(select, x, s, 10)
+
+
+@gpu
 def test_two_streams_and_a_captured_graph(select):
     from attention_decoder_b200 import _lib as L
     (x1, s1), (x2, s2) = draw(4, 4, 30000, 8), draw(4, 4, 30000, 9)
