@@ -16,9 +16,10 @@ constexpr int BM_THREADS = 256;
 constexpr int BM_WARPS = BM_THREADS / 32;
 constexpr int BM_CAP = 256;  // candidates of a part above its threshold that are ranked directly
 
-// Order-preserving map of finite floats and infinities to unsigned (NaN is mapped by the callers).
+// Order-preserving map of finite floats and infinities to unsigned (NaN is mapped by the callers). Zeros of either sign are one
+// value: -0 + 0 is +0.
 DEVI uint32_t ord_f(float x) {
-  const uint32_t u = __float_as_uint(x);
+  const uint32_t u = __float_as_uint(__fadd_rn(x, 0.f));
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 DEVI float unord_f(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
@@ -188,9 +189,9 @@ DEVI BeamBest shfl_best(BeamBest b, int o) {
 // bit; what is left is ranked all against all. Ties can leave too many all the same: then the lists merge head by head.
 constexpr int BM_MTHREADS = 512, BM_MWARPS = BM_MTHREADS / 32, BM_MERGE_CAP = 2048, BM_RANK_CAP = 512;
 
-// Order-preserving map of doubles (no NaN).
+// Order-preserving map of doubles (no NaN; zeros as in ord_f).
 DEVI uint64_t ord_d(double x) {
-  const uint64_t u = (uint64_t)__double_as_longlong(x);
+  const uint64_t u = (uint64_t)__double_as_longlong(__dadd_rn(x, 0.0));
   return u >> 63 ? ~u : u | (1ull << 63);
 }
 DEVI double unord_d(uint64_t k) { return __longlong_as_double((long long)(k >> 63 ? k & ~(1ull << 63) : ~k)); }

@@ -162,6 +162,21 @@ def test_a_nan_among_masked_tokens_counts(select):
 
 
 @gpu
+def test_zeros_of_either_sign_tie(select):
+    x = torch.tensor([[[-0.0, 0.0]]], device="cuda")
+    check(select, x, torch.zeros(1, 1, device="cuda"), 1)
+    x, s = draw(2, 2, 700, 23)
+    x = -x.abs() - 1
+    x[:, :, 100:400] = 0.0
+    x[:, :, 100:400:2] = -0.0                                   # 300 ties in a part: more than are ranked directly
+    check(select, x, s, 24)
+    x[:, :, 120:400] = -7.0
+    check(select, x, s, 9)
+    both = torch.ones(2, 2, dtype=torch.int32, device="cuda")
+    check(select, x, torch.tensor([[-0.0, 0.0], [0.0, -0.0]], device="cuda"), 1, done=both)
+
+
+@gpu
 def test_two_streams_and_a_captured_graph(select):
     from attention_decoder_b200 import _lib as L
     (x1, s1), (x2, s2) = draw(4, 4, 30000, 8), draw(4, 4, 30000, 9)
