@@ -6,6 +6,7 @@ import ctypes as C
 import torch
 
 from . import _lib as L
+from .model import outputs_for
 
 
 def _ptr(t):
@@ -29,15 +30,15 @@ def beam_select(logits, scores, n_out, done=None, end_token=0, out=None, workspa
             raise ValueError(f"scores and done must be contiguous [{G}, {B}], fp32 and int32, beside the logits")
     dev = logits.device
     if out is None:
-        out = {"score": torch.empty(G, n_out, dtype=torch.float32, device=dev),
-               "parent": torch.empty(G, n_out, dtype=torch.int32, device=dev),
-               "token": torch.empty(G, n_out, dtype=torch.int32, device=dev)}
+        out = dict(zip(("score", "parent", "token"), outputs_for(stream, lambda: [
+            torch.empty(G, n_out, dtype=kind, device=dev) for kind in (torch.float32, torch.int32, torch.int32)])))
     for n, kind in (("score", torch.float32), ("parent", torch.int32), ("token", torch.int32)):
         t = out[n]
         if t.shape != (G, n_out) or t.dtype != kind or t.device != dev or not t.is_contiguous():
             raise ValueError(f"out[{n!r}] must be contiguous [{G}, {n_out}] {kind} beside the logits")
     if workspace is None:
-        workspace = torch.empty(max(16, L.lfm3_beam_workspace(G, B, V, n_out)), dtype=torch.uint8, device=dev)
+        (workspace,) = outputs_for(stream, lambda: (torch.empty(max(16, L.lfm3_beam_workspace(G, B, V, n_out)), dtype=torch.uint8,
+                                                                device=dev),))
     with torch.cuda.device(dev):
         s = torch.cuda.current_stream() if stream is None else stream
         L.check(L.lfm3_beam_select(G, B, V, n_out, _ptr(logits), ld, _ptr(scores), _ptr(done), int(end_token), _ptr(out["score"]),

@@ -37,6 +37,19 @@ def _stream(stream):
     return C.c_void_p(s.cuda_stream)
 
 
+def outputs_for(stream, make):
+    """make()'s tensors, outputs of a call on ``stream`` (None: the current one). Memory comes from the stream that writes it
+    first, so that no pending work still has it, and once dropped it waits for the present stream too, which may read them."""
+    if stream is None:
+        return make()
+    now = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = make()
+    for t in out:
+        t.record_stream(now)
+    return out
+
+
 class Lfm3Model:
     """One decoder on one GPU. ``weights`` is ``lfm3_inputs.make_weights(...)``'s dict."""
 
@@ -159,41 +172,40 @@ class Lfm3Model:
         check(L.lfm3_restore(self.ctx, C.byref(st.struct), slot, _ptr(buf), buf.numel(), at, _stream(stream)), self.ctx)
 
     def _rows(self, st, q, k, v, gate):
-        """Checks one layer's rows and returns (their count, an output)."""
+        """Checks one layer's rows and returns their count."""
         g, dev = self.geom, st.seq_len.device
         n = int(q.shape[0])
         for name, t, shape, kind in (("q", q, (n, g.n_q, g.head_dim), torch.bfloat16), ("k", k, (n, g.n_kv, g.head_dim), torch.bfloat16),
                                      ("v", v, (n, g.n_kv, g.head_dim), torch.bfloat16), ("gate", gate, (n, g.n_q), torch.float32)):
             if tuple(t.shape) != shape or t.dtype != kind or t.device != dev or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {kind} tensor {shape} on {dev}")
-        return n, torch.empty_like(q)
+        return n
 
     def kv_attend(self, st, layer, slots, q, k, v, gate, W=1, d_slots=None, stream=None):
         """W rows of every listed slot enter and attend over one layer's 8-bit cache (see lfm3_kv_attend); returns y."""
         h_slots = np.ascontiguousarray(slots, dtype=np.int32)
-        n, y = self._rows(st, q, k, v, gate)
+        n = self._rows(st, q, k, v, gate)
         if n != len(h_slots) * W:
             raise ValueError(f"{n} rows are not {len(h_slots)} slots x {W}")
         if d_slots is None:
             d_slots = torch.from_numpy(h_slots).to(q.device)
         elif d_slots.shape != h_slots.shape or d_slots.dtype != torch.int32 or d_slots.device != q.device or not d_slots.is_contiguous():
             raise ValueError(f"d_slots must be a contiguous int32 tensor of {len(h_slots)} slots on {q.device}")
+        (y,) = outputs_for(stream, lambda: (torch.empty_like(q),))
         with torch.cuda.device(self.device):
             check(L.lfm3_kv_attend(self.ctx, C.byref(st.struct), layer, len(h_slots), _i32(h_slots), _ptr(d_slots), W, _ptr(q), _ptr(k),
                                    _ptr(v), _ptr(gate), _ptr(y), _stream(stream)), self.ctx)
-        if stream is not None:  # the caching allocator may not hand these out again before the call has run
+        if stream is not None:  # the caching allocator may not hand it out again before the call has run
             d_slots.record_stream(stream)
-            y.record_stream(stream)
         return y
 
     def kv_attend_prompt(self, st, layer, slot, q, k, v, gate, stream=None):
         """A prompt chunk's rows of one slot over one layer's 8-bit cache (see lfm3_kv_attend_prompt); returns y."""
-        n, y = self._rows(st, q, k, v, gate)
+        n = self._rows(st, q, k, v, gate)
+        (y,) = outputs_for(stream, lambda: (torch.empty_like(q),))
         with torch.cuda.device(self.device):
             check(L.lfm3_kv_attend_prompt(self.ctx, C.byref(st.struct), layer, slot, n, _ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(y),
                                           _stream(stream)), self.ctx)
-        if stream is not None:
-            y.record_stream(stream)
         return y
 
     def copy_pages(self, st, src, dst, stream=None):

@@ -177,6 +177,30 @@ def test_zeros_of_either_sign_tie(select):
 
 
 @gpu
+def test_outputs_on_another_stream_are_not_handed_out_early(select):
+    """The memory of outputs on a side stream: what is dropped before the call has run is not another tensor's yet, and what a
+    pending write on the current stream still has is not an output's."""
+    x, s = draw(4, 4, 3000, 24)
+    want = select(x, s, 64)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    del_me = select(x, s, 64, stream=side)
+    del del_me
+    others = [torch.full((4, 64), 7, dtype=torch.int32, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(bool((t == 7).all()) for t in others)
+    del others
+    torch.cuda._sleep(50_000_000)
+    others = [torch.full((4, 64), 7, dtype=torch.int32, device="cuda") for _ in range(2000)]  # all the free memory of that size
+    del others
+    got = select(x, s, 64, stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[n], want[n]) for n in want)
+
+
+@gpu
 def test_two_streams_and_a_captured_graph(select):
     from attention_decoder_b200 import _lib as L
     (x1, s1), (x2, s2) = draw(4, 4, 30000, 8), draw(4, 4, 30000, 9)
