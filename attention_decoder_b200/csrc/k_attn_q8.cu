@@ -4,8 +4,10 @@
 // is exactly one m16 operand of the warp MMA and its scale leaves the product: q.k = s_k (q.c), and the tile's share of
 // the output is s_v (p.c). The codes become f16 operands without rounding (1024 + 128 + c is put together by byte
 // permutes, 1152 subtracted in f16), the sums stay fp32. Queries are bf16 values held in f16 (exact from 2^-14 to
-// 65504 in size); probabilities are rounded to f16 (2^-11 relative, against the output's bf16 2^-8). The block that
-// a row lies in itself is attended in bf16 from the tail ring, its probabilities split into two bf16 halves (2^-16).
+// 65504 in size). Probabilities, relative to the warp's reference, are rounded to f16 after a factor of 2^7: 2^-11 relative
+// (against the output's bf16 2^-8) for those of 2^-21 and more, below that 2^-32 absolute a key, 2^-14 in all for the 2^18
+// keys that a warp has at most. The block that a row lies in itself is attended in bf16 from the tail ring, its probabilities
+// split into two bf16 halves (2^-16).
 //
 // Decode (k_kv8_attend): HBM bounds it at 1026 bytes a key and layer (4 heads x 256 B of codes + 2 B of scales). One
 // grid of resident blocks takes shares of all pages x kv heads of the batch, whatever the streams' lengths: whole shares of
@@ -357,6 +359,7 @@ __global__ void __launch_bounds__(Q8_THREADS, Q8Shape<NT>::RESIDENT)
   for (int k = 0; k < D; ++k) fetch(k, 0, k);
   uint32_t par = 0;  // phase of each ring slot's barrier
   const float sl2 = rsqrtf((float)HD) * 1.4426950408889634f;  // scores in base 2
+  constexpr float P_DOWN = 0x1p-7f;  // takes P_UP = 2^7 out again: with the values' scale, in the tail and in the sums
   bool ok = true;
   int k = 0, at = 0;  // tile, its place in the ring
   for (int r = lo; r < hi;) {  // segments
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(Q8_THREADS, Q8Shape<NT>::RESIDENT)
     for (int j = 0; j < NT; ++j) own[j] = (pr + min(2 * j + (t >> 1), nr - 1)) / QBLK;
 
     float o[NT][8][4];               // rows: dims 16 g + 2 i, + 1; columns 2t, 2t + 1
-    float mrun[NT][2], lrun[NT][2];  // per column; lrun: this lane's keys only
+    float mrun[NT][2], lrun[NT][2];  // per column: reference, 7 below a score (P_UP), and this lane's keys' sum
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -397,15 +400,15 @@ __global__ void __launch_bounds__(Q8_THREADS, Q8Shape<NT>::RESIDENT)
       mrun[j][0] = mrun[j][1] = -INFINITY;
       lrun[j][0] = lrun[j][1] = 0.f;
     }
-    // Online softmax of one tile's scores c (base 2, masked to -inf): c becomes the probabilities. The reference that is
-    // subtracted moves, and o is rescaled, only when a score exceeds it by more than 8 (probabilities up to 2^8 fit in f16), so
-    // that most tiles need one vote instead of a maximum over the lanes.
+    // Online softmax of one tile's scores c (base 2, masked to -inf): c becomes the probabilities times P_UP. The reference that
+    // is subtracted moves, and o is rescaled, only when a score is more than 8 above the one it was made of (times P_UP, that is
+    // 2^15, within f16), so that most tiles need one vote instead of a maximum over the lanes.
     auto softmax = [&](float (&c)[NT][4]) {
       bool grows = false;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) grows |= fmaxf(c[j][e], c[j][2 + e]) > mrun[j][e] + 8.f;
+        for (int e = 0; e < 2; ++e) grows |= fmaxf(c[j][e], c[j][2 + e]) - mrun[j][e] > 15.f;
       if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -415,7 +418,7 @@ __global__ void __launch_bounds__(Q8_THREADS, Q8Shape<NT>::RESIDENT)
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            m = fmaxf(m, mrun[j][e]);
+            m = fmaxf(m - 7.f, mrun[j][e]);
             const float al = m == -INFINITY ? 1.f : ex2(mrun[j][e] - m);
             mrun[j][e] = m;
             lrun[j][e] *= al;
@@ -443,6 +446,7 @@ __global__ void __launch_bounds__(Q8_THREADS, Q8Shape<NT>::RESIDENT)
     auto tile = [&](uint32_t kt, float ks, float vs, int u, auto every) {
       const uint32_t vt = kt + Q8_TILE;
       ks *= sl2;
+      vs *= P_DOWN;
       float c[NT][4], c2[NT][4];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -601,7 +605,7 @@ __global__ void __launch_bounds__(Q8_THREADS, Q8Shape<NT>::RESIDENT)
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float p = c[j][2 * e], q = c[j][2 * e + 1], hp = round_bf(p), hq = round_bf(q);
+            const float p = c[j][2 * e] * P_DOWN, q = c[j][2 * e + 1] * P_DOWN, hp = round_bf(p), hq = round_bf(q);
             ph[j][e] = movmatrix_t(pack_bf2(hp, hq));
             pl[j][e] = movmatrix_t(pack_bf2(p - hp, q - hq));
           }
@@ -644,8 +648,9 @@ __global__ void __launch_bounds__(Q8_THREADS, Q8Shape<NT>::RESIDENT)
         const int col = 8 * j + 2 * t + e;
         if (g == 0) {
           // NaN scores leave the maximum alone: a warp that saw nothing else still has to count
-          wm[warp][col] = l != l ? fmaxf(mrun[j][e], 0.f) : mrun[j][e];
-          wl[warp][col] = l;
+          const float m = mrun[j][e] + 7.f;
+          wm[warp][col] = l != l ? fmaxf(m, 0.f) : m;
+          wl[warp][col] = l * P_DOWN;
         }
         if (col < 4 * nr) {
           float* ob = obuf + ((size_t)warp * S::COLS + col) * HD + 16 * g;
