@@ -39,6 +39,8 @@ def beam_select(logits, scores, n_out, done=None, end_token=0, out=None, workspa
     if workspace is None:
         (workspace,) = outputs_for(stream, lambda: (torch.empty(max(16, L.lfm3_beam_workspace(G, B, V, n_out)), dtype=torch.uint8,
                                                                 device=dev),))
+    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous uint8 beside the logits")
     with torch.cuda.device(dev):
         s = torch.cuda.current_stream() if stream is None else stream
         L.check(L.lfm3_beam_select(G, B, V, n_out, _ptr(logits), ld, _ptr(scores), _ptr(done), int(end_token), _ptr(out["score"]),

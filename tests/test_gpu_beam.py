@@ -201,6 +201,23 @@ def test_outputs_on_another_stream_are_not_handed_out_early(select):
 
 
 @gpu
+def test_a_workspace_that_is_not_scratch_is_refused(select):
+    """(On the host: none of these reaches a kernel.)"""
+    from attention_decoder_b200 import _lib as L
+    x, s = draw(2, 4, 3000, 25)
+    n = L.lfm3_beam_workspace(2, 4, 3000, 8)
+    want = select(x, s, 8)
+    for ws in (torch.empty(n, dtype=torch.uint8), torch.empty(n, device="cuda"), torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            select(x, s, 8, workspace=ws)
+    with pytest.raises(L.Lfm3Error, match="workspace") as e:
+        select(x, s, 8, workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == -3
+    got = select(x, s, 8, workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))
+    assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+@gpu
 def test_two_streams_and_a_captured_graph(select):
     from attention_decoder_b200 import _lib as L
     (x1, s1), (x2, s2) = draw(4, 4, 30000, 8), draw(4, 4, 30000, 9)
