@@ -42,8 +42,15 @@ class Lfm3Pages:
             raise L.Lfm3Error(-3, f"{n} pages are needed, {len(free)} of {len(self.refs)} are free")
         return free[:n].astype(np.int32)
 
+    def _check(self, slot):
+        if not 0 <= slot < self.h.shape[0]:  # (numpy counts negative ones from the end)
+            raise L.Lfm3Error(-1, f"slot {slot} outside 0..{self.h.shape[0] - 1}")
+
     def lease(self, slot: int, positions: int, stream=None):
         """Makes sure that positions [0, positions) of ``slot`` have pages. Nothing changes on LFM3_E_CAPACITY."""
+        self._check(slot)
+        if positions < 0:
+            raise L.Lfm3Error(-1, f"{positions} positions")
         need = (positions + PAGE - 1) // PAGE
         if need > self.h.shape[1]:
             raise L.Lfm3Error(-3, f"{positions} positions exceed the slot's {self.h.shape[1]} pages")
@@ -57,6 +64,7 @@ class Lfm3Pages:
 
     def release(self, slot: int, stream=None):
         """Frees the slot for a new sequence: its pages lose one holder each, its length and conv columns become 0."""
+        self._check(slot)
         row = self.h[slot]
         np.subtract.at(self.refs, row[row >= 0], 1)
         row[:] = -1
