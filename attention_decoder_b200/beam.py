@@ -62,6 +62,15 @@ def beam_search(pages, prompt, n_beams, max_new, end_token=None, slots=None):
     slots = list(range(n_beams)) if slots is None else [int(s) for s in slots]
     if len(slots) != n_beams or n_beams < 1 or max_new < 1:
         raise ValueError("beam_search needs n_beams slots, and n_beams and max_new of at least 1")
+    # all of it before the slots lose what they hold
+    cfg = model.cfg
+    if len(set(slots)) != n_beams or not all(0 <= s < cfg.max_streams for s in slots):
+        raise ValueError(f"slots must be different ones of 0..{cfg.max_streams - 1}")
+    if n_beams > 64 or (max_new > 1 and n_beams > cfg.max_batch):
+        raise ValueError(f"{n_beams} beams are more than 64 or than the model's max_batch of {cfg.max_batch}")
+    if (prompt.dim() != 1 or len(prompt) < 1 or prompt.dtype != torch.int32 or prompt.device != pages.state.seq_len.device
+            or not prompt.is_contiguous()):
+        raise ValueError(f"prompt must be contiguous int32 [n] on {pages.state.seq_len.device}")
     with torch.cuda.device(model.device):
         return _search(pages, prompt, n_beams, max_new, end_token, slots)
 
