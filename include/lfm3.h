@@ -152,7 +152,8 @@ typedef struct {
  * code is x / s rounded to the nearest integer (ties to even), in [-127, 127]; it stands for
  * s * code. (x and s have 8-bit mantissas, so the fp32 quotient is never rounded across a tie: the
  * codes are those of exact arithmetic.) A block of zeros has s = 0; a block that holds a NaN or an
- * infinity has s = NaN, so the rows that see it become NaN as they would in bf16. A decode or
+ * infinity has s = NaN, so the rows that see it become NaN (in bf16 an infinite key can also be one
+ * without weight: a score of minus infinity). A decode or
  * verify row sees the earlier blocks in 8 bits and the block that it lies in itself in bf16; the
  * rows of a prompt chunk see the whole blocks before the chunk in 8 bits and everything after in
  * bf16. The fields are ignored (may be NULL) with LFM3_KV_BF16. */
@@ -357,7 +358,9 @@ lfm3_status lfm3_restore(lfm3_ctx* ctx, const lfm3_state* st, int slot, const vo
  * lfm3_kv_attend_prompt: n rows (1..max_chunk) of one slot; the open block's rows replace those in
  * the slot's tail. The slot's keys and values are laid out in bf16 in the workspace. A captured call is
  * for the position that h_seq_len had.
- * A row that sees a key or a value that is not finite becomes NaN in all its dims of that kv head.
+ * A row that sees a value that is not finite, a key that is NaN, or in 8 bits a block with either or
+ * with an infinite key becomes NaN in all its dims of that kv head. An infinite key that is seen in
+ * bf16 makes an infinite score: NaN with a positive one, no weight with a negative one.
  * Errors (nothing enqueued): LFM3_E_UNSUPPORTED with a bf16 pool; LFM3_E_ARG for a layer that is not a
  * full-attention one, a NULL or misaligned pointer, a bad or repeated slot, W, n or rows out of range;
  * LFM3_E_CAPACITY if a slot's pages cannot hold the rows; LFM3_E_STATE before lfm3_bind_workspace. Both
