@@ -204,6 +204,23 @@ def test_other_streams_and_captured_calls(lib, weights, fmt):
         assert torch.equal(getattr(st, n).view(torch.uint8), ref.view(torch.uint8))
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+def test_a_captured_reorder_moves_when_it_is_replayed(lib, weights, fmt):
+    m = lib(weights, max_streams=3, max_pages_per_stream=2, n_pages=10, max_chunk=64, kv_format=fmt)
+    st = random_state(m, [70, 100, 20], 8)
+    free = sorted(set(range(10)) - set(st.h_page_table.reshape(-1).tolist()))
+    before = snapshot(st)
+    want = reordered(st, [0, 1, 2], [1, 0, 1], free, fmt == "int8")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.reorder(st, [0, 1, 2], [1, 0, 1], free[:3])
+    torch.cuda.synchronize()
+    for n in NAMES:
+        assert before[n] is None or torch.equal(getattr(st, n), before[n]), n
+    graph.replay()
+    same(st, want)
+
+
 def test_arrays_that_are_not_aligned_are_refused(lib, weights):
     from attention_decoder_b200 import Lfm3Error
     m = lib(weights, max_streams=2, max_pages_per_stream=1, max_chunk=64)
@@ -294,6 +311,41 @@ def test_forked_reordered_and_compacted_slots_decode_like_unshared_ones(lib):
     for s in range(4):
         m.prefill(plain, s, tokens=prompt)
     for i in range(12):
+        ref = m.decode(plain, range(4), tokens=torch.tensor([h[i] for h in history], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(out["logits"], ref["logits"])
+    m.check_device_errors()
+
+
+def test_forked_reordered_and_compacted_slots_with_an_8_bit_pool(lib):
+    """The same over 8-bit codes: states of the same lengths split their keys alike, so the bits are the same too."""
+    from attention_decoder_b200 import Lfm3Pages
+    g = lfm3_1p7b(layer_types=(0, 2, 1, 1))
+    m = lib(make_weights(g, 0), max_streams=4, max_pages_per_stream=6, n_pages=40, max_batch=4, kv_format="int8")
+    prompt = torch.from_numpy(make_tokens(1, "fork8", 117, g.vocab)).cuda()
+    tok = make_tokens(2, "fork8.steps", 4 * 30, g.vocab).reshape(30, 4)
+    st = m.new_state(poison=True)
+    pool = Lfm3Pages(st)
+    pool.lease(1, 117)
+    m.prefill(st, 1, tokens=prompt)
+    pool.fork(1, [0, 2, 3])
+    history = [[] for _ in range(4)]
+    maps = {3: [2, 0, 1, 1], 11: [1, 2, 3, 0], 12: [0, 3, 3, 3], 20: [3, 3, 0, 2]}  # at 120, 128 (a block and a page full), 129, 137
+    for i in range(30):
+        if i in maps:
+            pool.reorder(range(4), maps[i])
+            history = [list(history[p]) for p in maps[i]]
+        if i in (9, 21):
+            pool.compact()
+        for s in range(4):
+            pool.lease(s, int(st.h_seq_len[s]) + 1)
+            history[s].append(int(tok[i, s]))
+        out = m.decode(st, range(4), tokens=torch.from_numpy(tok[i]).cuda())
+        holders(pool)
+    plain = m.new_state(page_table=np.arange(24).reshape(4, 6))
+    for s in range(4):
+        m.prefill(plain, s, tokens=prompt)
+    for i in range(30):
         ref = m.decode(plain, range(4), tokens=torch.tensor([h[i] for h in history], dtype=torch.int32, device="cuda"))
     torch.cuda.synchronize()
     assert torch.equal(out["logits"], ref["logits"])
