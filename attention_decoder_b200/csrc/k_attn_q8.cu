@@ -17,8 +17,8 @@
 // warps owns one quarter of every page, i.e. whole 16-key tiles, streams them by TMA through its own ring of buffers across
 // segment borders (evict-first in L2: read once, and the lengths, tables, queries and parts stay), and keeps its own online
 // softmax; they meet only where a segment ends, while the SM's other blocks keep the memory busy.
-// Measured (one layer, graph of calls over three caches): one stream at 2047 keys 10.6 us, at 131000 34.6 us (134 MB, 3.9 TB/s),
-// 64 streams at 256..8191 59.2 us (278 MB, 4.7 TB/s), at 8000 96 us (526 MB, 5.5 TB/s), 13 windows of 4 rows at 500..8100 27.5 us.
+// Measured (one layer, graph of calls over three caches): one stream at 2047 keys 10.7 us, at 131000 34.6 us (134 MB, 3.9 TB/s),
+// 64 streams at 256..8191 59.3 us (278 MB, 4.7 TB/s), at 8000 96 us (526 MB, 5.5 TB/s), 13 windows of 4 rows at 500..8100 27.4 us.
 // 64 streams at 8000 take 39.5 us more than at 4000: 6.7 TB/s while it streams. The rest is latency: 4 us to the first tile
 // (lengths, table, tile: three dependent reads), 6 to 8 us of merges behind the last, 2 to 4 us at a second segment. Windows
 // are bound by the warps' instructions (two n-tiles: 8 warps an SM).
@@ -32,8 +32,9 @@ namespace lfm3 {
 
 constexpr int Q8_WARPS = 4, Q8_THREADS = 32 * Q8_WARPS;
 constexpr int Q8_TILE = QBLK * HD;  // bytes of a tile of codes, K or V
-// A block's share where there is little to share. With 1, 2, 3 pages: 13 windows of 3 rows at 100 keys 17.2, 15.0, 15.0 us, 2 at
-// 3300..5200 20.2, 20.2, 21.5 us (and 40 at 5).
+// A block's share, in pages, where there is little to share: fewer parts have fewer levels of merges, more parts shorter loops. With
+// 2, 3, 4 pages one stream takes at 300 keys 8.3, 8.9, 8.9 us, at 1000 8.7, 9.0, 9.9, at 2047 10.9, 10.8, 10.8, at 4000 10.4, 11.2, 11.2;
+// 4 streams at 2047 12.8, 12.3, 11.8; 2 windows of 3 rows at 3300..5200 16.0, 17.0, 16.7.
 constexpr int Q8_MIN_PAGES = 2;
 static_assert(PAGE == Q8_WARPS * QBLK, "a warp owns one quarter of every page");
 
@@ -158,10 +159,10 @@ DEVI void q8_store_rows(const Q8Attend& A, int stream, int kvh, int isv, int lan
     reinterpret_cast<uint2*>(tail + (size_t)((p0 + i) % QRING) * HD)[lane] = __ldcg(reinterpret_cast<const uint2*>(R.at(p0 + i)) + lane);
 }
 
-// NT: n-tiles of 8 columns = 2 rows x 4 heads each. Two of them take 255 registers: with three blocks an SM (168 registers, 300
-// bytes spilled) 13 windows of 4 rows took 55 us instead of 35. Four tiles in flight instead of three: 29.7 against 28.8.
+// NT: n-tiles of 8 columns = 2 rows x 4 heads each. Two of them take 254 registers, so two blocks an SM (three, with 300 bytes
+// spilled, made 13 windows of 4 rows half as long again). A fourth tile in flight does not help (3 % slower).
 // SEGMENT: 3, 4, 6, 8 pages gave 63.1, 62.5, 62.8, 64.1 us for 64 streams at 256..8191 and 33.5, 31.8, 30.8, 30.8 for 3 at
-// 23000..43000; with two n-tiles 6, 10, 12 gave 30.5, 28.8, 28.8.
+// 23000..43000; with two n-tiles 6, 10, 12 pages gave 30.5, 28.8, 28.8 for 13 windows of 4 rows.
 template <int NT>
 struct Q8Shape {
   static constexpr int RESIDENT = NT == 1 ? 3 : 2;  // blocks per SM
@@ -234,9 +235,9 @@ __global__ void __launch_bounds__(Q8_THREADS, Q8Shape<NT>::RESIDENT)
   // A block for whole shares of one segment: of `per` pages at most, the fewest with which the blocks suffice ..
   const int n0 = lane < A.streams ? pages_of(lane) : 0, n1 = lane + 32 < A.streams ? pages_of(lane + 32) : 0;  // (this lane's)
   {
-    // .. if that is no more than a block's part (in pages, a further segment's cost included) of equal shares: 61 streams at
-    // 51..86 took 20 us with equal shares and 11.4 with whole ones, 64 at 256..8191 (54 pages instead of 42) 68 and 80. (There
-    // are more blocks than segments, so `per` = P would do for any batch.)
+    // .. if that is no more than a block's part (in pages, a further segment's cost included) of equal shares. 61 streams at
+    // 51..86 take 11.4 us with whole shares, 20 with equal ones. 64 at 256..8191 take 80 us with whole shares (of 54 pages), 68
+    // with equal ones (of 42). (There are more blocks than segments, so `per` = P would do for any batch.)
     const int least = max(Q8_MIN_PAGES, (P + G - 1) / G), most = P < 2 * G ? P : (P + S::SEGMENT * hg * A.streams) / G;
     int found = INT_MAX;
     for (int s = least + warp; s <= most && found == INT_MAX; s += Q8_WARPS)
@@ -625,7 +626,8 @@ __global__ void __launch_bounds__(Q8_THREADS, Q8Shape<NT>::RESIDENT)
         }
       }
     }
-    // the rest, in a loop of its own (no masks, no other code between): 64 streams 59.2 us instead of 63.1, windows 7 % less
+    // the rest, in a loop of its own (no masks, no other code between). 64 streams at 256..8191 take 59.2 us instead of 63.1, windows
+    // 7 % less; one stream at 2047 keys takes 10.6 instead of 9.9 (4 of the 1017 us of a whole token).
     for (; lo + k < end; next_tile()) {
       if (!ok) continue;
       ok = __all_sync(0xffffffffu, mbar_wait(su32(&bars[warp][at]), (par >> at) & 1, A.err));

@@ -16,7 +16,8 @@ class Lfm3Pages:
     """Page pool of one ``Lfm3State``. Takes over the state's page table: every slot starts without pages.
 
     The full pages of a forked slot are shared with its source; the partly filled page that the next position goes to
-    belongs to one slot alone. All methods follow the host's view of the lengths (``state.h_seq_len``) and enqueue
+    belongs to one slot alone. A call that writes positions below a slot's length (``restore``) needs pages of its own there:
+    ``release`` and ``lease`` come first. All methods follow the host's view of the lengths (``state.h_seq_len``) and enqueue
     their device work on ``stream`` (default: torch's current stream)."""
 
     def __init__(self, state, stream=None):

@@ -330,7 +330,9 @@ lfm3_status lfm3_keep(lfm3_ctx* ctx, const lfm3_state* st, int slot, void* d_sna
 
 /* Restores a state kept at mark `at` into `slot`: conv columns and rings are overwritten, the
  * kept pages are written into the slot's own pages (through its page table), and seq_len[slot]
- * and h_seq_len[slot] become `at`. The slot's previous contents are discarded. Errors:
+ * and h_seq_len[slot] become `at`. The slot's previous contents are discarded. (Pages that the slot
+ * has shared with others since an lfm3_reorder would change for those too: it needs pages of its own
+ * first.) Errors:
  * LFM3_E_CAPACITY if the slot's pages cannot hold [0, at) or the buffer is too small (TensorFold
  * PR #1508, pool-leasing commit: "forward refuses rows past a slot's pages"); LFM3_E_ARG for a
  * bad slot, buffer or mark. Nothing is enqueued and no state is touched on error. */
