@@ -650,9 +650,8 @@ __global__ void __launch_bounds__(Q8_THREADS, Q8Shape<NT>::RESIDENT)
         const int col = 8 * j + 2 * t + e;
         if (g == 0) {
           // NaN scores leave the maximum alone: a warp that saw nothing else still has to count
-          const float m = mrun[j][e] + 7.f;
-          wm[warp][col] = l != l ? fmaxf(m, 0.f) : m;
-          wl[warp][col] = l * P_DOWN;
+          wm[warp][col] = l != l ? fmaxf(mrun[j][e], 0.f) : mrun[j][e];
+          wl[warp][col] = l * P_DOWN;  // (as the outputs: relative to the reference and P_UP, the same for all states)
         }
         if (col < 4 * nr) {
           float* ob = obuf + ((size_t)warp * S::COLS + col) * HD + 16 * g;
