@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
               const int k = half * (PA_KT / 16 / PA_HALVES) + i;
               pa_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, vd + k * 128, idesc_o, (j | k) != 0);
             }
-            if (half == PA_HALVES - 1 && t == 1) pa_commit(kv_empty + 8 * st);
+            // (a stage that no later tile takes is not given back: nothing would wait for that arrival)
+            if (half == PA_HALVES - 1 && t == 1 && j + 2 < nt) pa_commit(kv_empty + 8 * st);
             if (half == PA_HALVES - 1 && !more) pa_commit(o_done + 8 * t);
           }
           __syncwarp();
