@@ -1637,19 +1637,18 @@ extern "C" lfm3_status lfm3_reorder(lfm3_ctx* ctx, const lfm3_state* st, int n, 
   a.pool = page_pool(ctx, st);
   a.table = paged ? const_cast<int32_t*>(st->page_table) : nullptr;
   a.seq_len = st->seq_len;
+  // the mirror's new rows, before anything is enqueued: nothing behind the launch can fail
+  std::vector<int32_t> rows(paged ? (size_t)a.n * mpp : 0, -1);
+  for (int m = 0; paged && m < a.n; ++m) {
+    const int last = a.len[m] / PAGE;
+    std::copy_n(table + (size_t)a.src[m] * mpp, last, rows.data() + (size_t)m * mpp);
+    if (last < mpp) rows[(size_t)m * mpp + last] = a.page_dst[m];
+  }
   g_launches = 0;
   CK(reorder_states(a, reinterpret_cast<cudaStream_t>(stream)));
   ctx->launches = g_launches;
   ctx->vw_n = 0;  // the slots of a verify window may have changed
-  if (paged) {
-    std::vector<int32_t> rows((size_t)a.n * mpp, -1);
-    for (int m = 0; m < a.n; ++m) {
-      const int last = a.len[m] / PAGE;
-      std::copy_n(table + (size_t)a.src[m] * mpp, last, rows.data() + (size_t)m * mpp);
-      if (last < mpp) rows[(size_t)m * mpp + last] = a.page_dst[m];
-    }
-    for (int m = 0; m < a.n; ++m) std::copy_n(rows.data() + (size_t)m * mpp, mpp, table + (size_t)a.dst[m] * mpp);
-  }
+  for (int m = 0; paged && m < a.n; ++m) std::copy_n(rows.data() + (size_t)m * mpp, mpp, table + (size_t)a.dst[m] * mpp);
   for (int m = 0; m < a.n; ++m) st->h_seq_len[a.dst[m]] = a.len[m];
   return LFM3_OK;
 }
